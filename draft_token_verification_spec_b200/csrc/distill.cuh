@@ -533,6 +533,16 @@ __global__ void __launch_bounds__(kThreads) distill_list_kernel(
   if ((threadIdx.x & 31) == 0) j.lists[row] = l;
 }
 
+// A block may write to another's shared memory only once that one runs: each says so as it starts, and
+// waits for its fellows before its first remote store, behind its list and under its tile's loads.
+// (Nothing is handed over here, so that the arrival is relaxed; the exchange has a barrier of its own.)
+__device__ __forceinline__ void cluster_arrive_started() {
+  asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait_started() {
+  asm volatile("barrier.cluster.wait;" ::: "memory");
+}
+
 struct DistillRowSmem {
   uint32_t marks[kTileVectors / 4];
   DistillPart part[kMaxRowBlocks * kWarps];  // the row's, in every block
@@ -546,7 +556,7 @@ __device__ __forceinline__ float weight_f(float x, float m, const Log2Scale& c) 
 }
 
 // A block does its tile's sums and sends its warps' parts to every block of the cluster; after the
-// cluster's one barrier every warp puts the row together for itself from its own block's shared
+// exchange's barrier every warp puts the row together for itself from its own block's shared
 // memory, in float32: the gradient's factors need no more, nor does the loss beside them. The
 // list's side comes from distill_list_kernel, which runs beside the tiles' loads (kList false),
 // or, in calls too small for a second launch to pay, from the first block's first warp (it would
@@ -556,6 +566,7 @@ __global__ void __launch_bounds__(kThreads, 6) distill_row_kernel(
     const __grid_constant__ DistillRowJob j) {
   __shared__ DistillRowSmem sm;
   __shared__ __align__(16) uint4 s_tile[kTileVectors];
+  cluster_arrive_started();
   cg::cluster_group cl = cg::this_cluster();
   const int n = j.n, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int row = int(blockIdx.x / unsigned(n)), tile = int(blockIdx.x % unsigned(n));
@@ -575,6 +586,7 @@ __global__ void __launch_bounds__(kThreads, 6) distill_row_kernel(
   if (kGrad && here) x = rv.entry(id);
   const int bad = mark_listed(sm.marks, rv, tile, id);
   const int to = kGrad ? n : 1;  // blocks that need the row's parts
+  cluster_wait_started();
   if (kList && tile == 0 && warp == 0) {
     const ListSide l = weigh_list(j.k, j.iT, j.ids + size_t(row) * j.k,
                                   j.values + size_t(row) * j.k, j.lse ? j.lse + row : nullptr,
