@@ -247,7 +247,8 @@ __device__ __forceinline__ ListSide weigh_list(int k, double iT, const int32_t* 
     scale = any ? exp(double(am) * iT - l.log_t) : 0.0;
     l.mass = ta * scale;
     l.rho = 1.0 - l.mass;
-    if (!(l.rho > (fabs(l.log_t) + 1.0) * 0x1.0p-23)) l.rho = 0.0;
+    // (a list without entries asks for nothing: no rest either)
+    if (!any || !(l.rho > (fabs(l.log_t) + 1.0) * 0x1.0p-23)) l.rho = 0.0;
   } else if (any) {
     l.log_t = double(am) * iT + log(ta);
     scale = 1.0 / ta;
