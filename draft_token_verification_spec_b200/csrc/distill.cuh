@@ -8,7 +8,9 @@
 // lse, (|lse| + 1) 2^-23) and sigma the student's:
 //   L = sum_j t_j (log t_j - log s_{i_j}) + rho (log rho - log sigma)
 //   dL/dz_v = (s_v - t_v) / T listed,  (sigma - rho) q_v / T unlisted,
-// q_v = s_v / sigma the student's share of its own rest. sigma comes from the sum over the
+// q_v = s_v / sigma the student's share of its own rest. That is L's derivative where
+// M = sum_j t_j + rho is 1; where an lse too small for its list makes M larger (rho is held at 0), the
+// loss counts its sum t_j and the gradient still counts 1. sigma comes from the sum over the
 // unlisted entries alone, never from 1 - sum_j s_{i_j}, which cancels when the student is sure.
 //
 // What bounds it: HBM. The loss reads a row once, the gradient reads and writes it once; the

@@ -335,6 +335,9 @@ spec_status spec_top_logits(const void* logits, spec_dtype dtype, int rows, int 
  *   loss = sum_j t_j (log t_j - log s_j) + rho (log rho - log sigma), sigma the student's mass
  *   outside the list (terms with t_j = 0 or rho = 0 are 0; +inf where the student has no mass);
  *   d loss / d z_v = (s_v - t_v) / temp listed, (s_v - rho s_v / sigma) / temp unlisted.
+ * Both take the teacher's masses for a distribution: sum_j t_j + rho = 1. With an lse too small for
+ * its list sum_j t_j exceeds 1 and rho is 0; the gradient then stays as stated, which is the loss's
+ * derivative less (sum_j t_j - 1) s_v / temp (softmax(z) - t: it sums to 1 - sum_j t_j over the row).
  * A list without entries asks for nothing: loss 0 (with teacher_lse too) and gradient 0.
  *   stats [rows][4] float (16-byte aligned): what the backward pass needs of the forward one:
  *     m, Z, m_rest, R = the largest logit and sum_v exp((z_v - m) / temp) over all entries,

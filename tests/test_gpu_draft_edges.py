@@ -37,3 +37,50 @@ def test_a_list_without_entries_costs_nothing(V, dtype, rows):
     x[1, 5] = math.nan               # still a row in error
     loss, grad = sv.spec_distill_loss_grad(x, ids, val, lse)
     assert torch.isnan(loss[1]) and torch.isnan(grad[1].float()).all() and (loss[2:] == 0.0).all()
+
+
+def loss_and_gradient(z, ids, val, lse, T):
+    """The loss over the whole vocabulary in double, its gradient by automatic differentiation, and
+    what the gradient's roundings are relative to (lists without padding)."""
+    z = z.double().cpu().requires_grad_(True)
+    at, a = ids.cpu().long(), val.double().cpu() / T
+    t = (a - lse.double().cpu()[:, None]).exp()
+    on = torch.zeros_like(z, dtype=torch.bool).scatter(1, at, True)
+    rho = 1.0 - t.sum(1)
+    rho = torch.where(rho > (lse.double().cpu().abs() + 1.0) * 2.0 ** -23, rho, 0.0)
+    logs = torch.log_softmax(z / T, 1)
+    log_sigma = torch.logsumexp(torch.where(on, -math.inf, logs), 1)
+    loss = (torch.xlogy(t, t) - t * logs.gather(1, at)).sum(1) + torch.xlogy(rho, rho) - rho * log_sigma
+    loss.sum().backward()
+    s = logs.detach().exp()
+    M = (t.sum(1) + rho)[:, None]
+    share = s / log_sigma.detach().exp()[:, None]
+    scale = torch.where(on, M * s + torch.zeros_like(s).scatter(1, at, t), M * s + rho[:, None] * share) / T
+    return loss.detach(), z.grad, scale
+
+
+@pytest.mark.parametrize("rows", [4, 180])
+@pytest.mark.parametrize("V,dtype,T,off", [(500, F32, 1.3, -0.3), (20000, BF16, 1.0, -1.5),
+                                           (30000, F32, 0.7, 0.4), (270000, BF16, 1.0, -0.2)])
+def test_a_log_sum_exp_that_is_not_the_list_s_own(V, dtype, T, off, rows):
+    """Masses of exp(-off) in all, with and without a rest: the loss counts them as they are, the
+    gradient as if they were 1, as the header states. Tolerances as in test_gpu_distill.py: the loss
+    1e-5 (1 + M), the gradient 1e-5 of M s + t."""
+    if V == 270000:
+        rows = min(rows, 4)
+    x = make(rows, V, dtype)
+    ids, val, _ = teacher(x, 20, short=False, T=T)
+    lse = torch.logsumexp(val.double() / T, 1).float() + off
+    rl, rg, scale = loss_and_gradient(x, ids, val, lse, T)
+    M = (val.double().cpu() / T - lse.double().cpu()[:, None]).exp().sum(1).clamp(min=1.0)
+    rg = rg - (M - 1.0)[:, None] * torch.softmax(x.double().cpu() / T, 1) / T
+    loss, stats = sv.spec_distill_loss(x, ids, val, lse, T)
+    both_loss, both_grad = sv.spec_distill_loss_grad(x, ids, val, lse, T)
+    grad = sv.spec_distill_grad(x, ids, val, lse, T, stats)
+    step = torch.finfo(dtype).eps / 2
+    for got in (loss, both_loss):
+        lim = 1e-5 * (1 + M) + 2.0 ** -23 * rl.abs()
+        assert ((got.double().cpu() - rl).abs() <= lim).all()
+    for got in (grad, both_grad):
+        lim = step * rg.abs() + (1 + step) * 1e-5 * scale + 2e-38
+        assert ((got.double().cpu() - rg).abs() <= lim).all()
