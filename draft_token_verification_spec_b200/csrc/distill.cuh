@@ -552,12 +552,6 @@ struct DistillRowSmem {
   ListSide list;
 };
 
-// exp((x - m) / T) in float32, x <= m.
-__device__ __forceinline__ float weight_f(float x, float m, const Log2Scale& c) {
-  const float d = x - m;
-  return ex2(fmaf(d, c.hi, d * c.lo));
-}
-
 // A block does its tile's sums and sends its warps' parts to every block of the cluster; after the
 // exchange's barrier every warp puts the row together for itself from its own block's shared
 // memory, in float32: the gradient's factors need no more, nor does the loss beside them. The

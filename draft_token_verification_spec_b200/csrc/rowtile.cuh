@@ -253,6 +253,12 @@ __device__ __forceinline__ Log2Scale log2_scale_row(float T) {
   return Log2Scale{hi, __fdividef(r, T)};
 }
 
+// exp((x - m) / T) in float32, x <= m.
+__device__ __forceinline__ float weight_f(float x, float m, const Log2Scale& c) {
+  const float d = x - m;
+  return ex2(fmaf(d, c.hi, d * c.lo));
+}
+
 // Sum of exp2((x - m) c) over the entries of one vector, m >= every entry and m > -inf. The
 // difference is taken first: it is exact where it matters, and -inf or the type's lowest value
 // minus m stays a number that weighs 0. Relative error of a weight: 2^-22 of ex2, and

@@ -892,6 +892,83 @@ __device__ __forceinline__ void write_top(const TopJob& j, int row, int i, bool 
   j.values[size_t(row) * j.k + i] = on ? pool_value(e) : -INFINITY;
 }
 
+// ------------------------------------------------------- the log-sum-exp of the top logits
+// A list that holds all of a row's mass must not leave any over when its masses are taken with the
+// row's log-sum-exp (the distillation loss would set it against a student that has none there). The
+// float32 sum of the tiles is off by up to e = sum_error of itself. Where it exceeds the k largest,
+// weighed in double, by more than 2 e there is mass outside them, and it stands. Else the sum is taken
+// again, part by part (a warp's 256 vectors of a tile): the parts that hold more than 1 / (128
+// parts) of it are read again, their entries among the k largest weigh in double, and only the rest
+// of them in float32. The other parts are 1/128 of the sum together: it is off by e / 128 < 2.1e-8.
+__device__ __forceinline__ bool sum_stands(int V, double S, double largest) {
+  return S - largest > 2.0 * sum_error(V, S) * S;
+}
+
+// The calling warp's share of that sum (each lane's is to be added): the parts and the k largest are
+// dealt out to `warps` warps. top: the row's largest entries in order, `have` of them, fewer than k
+// where no other is above -inf.
+template <typename T>
+__device__ __noinline__ double exact_share(const TileJob& t, const RowView<T>& rv, int row, float m,
+                                           double iT, const double* tab, const Log2Scale& sc,
+                                           const unsigned long long* top, int have, int k, double S,
+                                           int warp, int warps) {
+  constexpr int P = Elem<T>::kPerVec;
+  const int n = t.n, parts_n = n * kWarps, lane = threadIdx.x & 31;
+  const WarpPart* parts = t.parts + size_t(row) * parts_n;
+  const DoubleWeight f(m, iT, tab);
+  const double least = S / (128.0 * double(parts_n));
+  auto mass = [&](int i) {
+    const WarpPart p = parts[i];
+    return p.m > -INFINITY ? double(p.s) * f(p.m) : 0.0;
+  };
+  double share = 0.0;
+  const unsigned long long last = have >= k ? top[k - 1] : 0ull;
+  const float b = pool_value(last);
+#pragma unroll 1
+  for (int i0 = warp * 32; i0 < parts_n; i0 += warps * 32) {
+    const double w = i0 + lane < parts_n ? mass(i0 + lane) : 0.0;
+    uint32_t again = __ballot_sync(0xffffffffu, w > least);
+    if (!(w > least)) share += w;
+    if (last == 0ull) continue;  // (the others' rests hold nothing)
+#pragma unroll 1
+    for (; again; again &= again - 1u) {
+      const int i = i0 + __ffs(int(again)) - 1;
+      uint4 v[kTileVecs];
+#pragma unroll
+      for (int u = 0; u < kTileVecs; ++u) {
+        const int g = tile_vector_of(true, i / kWarps, n, u, i % kWarps, lane);
+        v[u] = g < rv.G ? rv.load(g) : neg_inf_vec(int(sizeof(T)));
+      }
+      float s = 0.0f;
+#pragma unroll
+      for (int u = 0; u < kTileVecs; ++u) {
+        float x[P], su = 0.0f;
+        Elem<T>::unpack(v[u], x);
+        const int e0 = rv.first(tile_vector_of(true, i / kWarps, n, u, i % kWarps, lane));
+#pragma unroll
+        for (int e = 0; e < P; ++e) {
+          const unsigned long long at = ((unsigned long long)f32_key(x[e]) << 32) |
+                                        (unsigned long long)(0xFFFFFFFFu - uint32_t(e0 + e));
+          if (x[e] > -INFINITY && at < last) su += weight_f(x[e], b, sc);
+        }
+        s += su;
+      }
+      s = warp_sum_f32(s);
+      if (lane == 0) share += double(s) * f(b);
+    }
+  }
+#pragma unroll 1
+  for (int i = warp * 32 + lane; i < min(have, k); i += warps * 32) {
+    const int piece = (pool_id(top[i]) + rv.mis) / P / 32;  // dealt out to the tiles in turn
+    if (mass(piece % n * kWarps + piece / n % kWarps) > least) share += f(pool_value(top[i]));
+  }
+  return share;
+}
+
+__device__ __forceinline__ void write_lse(const TopJob& j, int row, float m, double iT, double S) {
+  j.lse[row] = float(double(m) * iT + log(S));
+}
+
 // ------------------------------------------------------- finishing by one warp
 // Rows that keep up to kShortK entries whatever the others weigh (spec_top_logits, one top-k for
 // all rows): their pools are mostly under 256 entries, and a warp sorts those in its registers with
@@ -1063,22 +1140,32 @@ __device__ __forceinline__ bool short_pool(const Job& j, const RowAsk& a, int ro
   return true;
 }
 
-__device__ __forceinline__ bool finish_short(const TopJob& j, const RowAsk& a, int row,
+template <typename T>
+__device__ __forceinline__ bool finish_short(const TopJob& j, const RowAsk& a,
+                                             const RowView<T>& rv, int row,
                                              unsigned long long* pool, double* w,
                                              const double* tab) {
   const int lane = threadIdx.x & 31;
   float m;
   double s;
   if (!short_pool(j, a, row, pool, tab, &m, j.lse ? &s : nullptr)) return false;
-  if (lane == 0) {
-    j.t.left[row] = RowLeft{0, 0.0f, 0u, 0u};
-    if (j.lse) j.lse[row] = float(double(m) * a.iT + log(s));
+  if (lane == 0) j.t.left[row] = RowLeft{0, 0.0f, 0u, 0u};
+  if (j.lse) {
+    const DoubleWeight f(m, a.iT, tab);
+    double own = 0.0;
+#pragma unroll 1
+    for (int i = lane; i < j.k; i += 32) own += f(pool_value(pool[i]));
+    if (!sum_stands(j.t.V, s, warp_sum_f64(own)))
+      s = warp_sum_f64(exact_share(j.t, rv, row, m, a.iT, tab, j.c, pool, j.k, j.k, s, 0, 1));
+    if (lane == 0) write_lse(j, row, m, a.iT, s);
   }
   for (int i = lane; i < j.k; i += 32) write_top(j, row, i, true, pool[i]);
   return true;
 }
 
-__device__ __forceinline__ bool finish_short(const SampleJob& j, const RowAsk& a, int row,
+template <typename T>
+__device__ __forceinline__ bool finish_short(const SampleJob& j, const RowAsk& a,
+                                             const RowView<T>&, int row,
                                              unsigned long long* pool, double* w,
                                              const double* tab) {
   const int lane = threadIdx.x & 31;
@@ -1281,11 +1368,9 @@ __device__ void finish_row(const TopJob& j, const RowAsk& a, const RowView<T>& r
                            PoolSmem& sm) {
   const int tid = threadIdx.x;
   merge_parts(j, a, row, sm);
-  if (tid == 0) {
-    j.t.left[row] = RowLeft{0, 0.0f, 0u, 0u};
-    if (j.lse) j.lse[row] = sm.bad ? NAN : float(double(sm.m) * a.iT + log(sm.s));
-  }
+  if (tid == 0) j.t.left[row] = RowLeft{0, 0.0f, 0u, 0u};
   if (sm.bad) {
+    if (tid == 0 && j.lse) j.lse[row] = NAN;
     for (int i = tid; i < j.k; i += kThreads) {
       j.ids[size_t(row) * j.k + i] = -1;
       j.values[size_t(row) * j.k + i] = NAN;
@@ -1322,6 +1407,16 @@ __device__ void finish_row(const TopJob& j, const RowAsk& a, const RowView<T>& r
     return;
   }
   for (int i = tid; i < j.k; i += kThreads) write_top(j, row, i, i < c, sm.e()[i < c ? i : 0]);
+  if (j.lse) {
+    static_assert(kMaxJ <= kThreads, "one of the k largest to a thread");
+    const DoubleWeight f(sm.m, a.iT, sm.tab);
+    double S = sm.s;
+    const double own = tid < min(c, j.k) ? f(pool_value(sm.e()[tid])) : 0.0;
+    if (!sum_stands(j.t.V, S, block_sum_f64(own, sm.scr)))
+      S = block_sum_f64(exact_share(j.t, rv, row, sm.m, a.iT, sm.tab, j.c, sm.e(), c, j.k, S,
+                                    tid >> 5, kWarps), sm.scr);
+    if (tid == 0) write_lse(j, row, sm.m, a.iT, S);
+  }
 }
 
 // The steps in a launch each.
@@ -1344,7 +1439,7 @@ __global__ void __launch_bounds__(kThreads, 4) row_finish_kernel(const __grid_co
   finish_row<T>(j, a, RowView<T>(j.t.logits, row, j.t.stride, j.t.V), row, pool);
 }
 template <typename T, typename Job>
-__global__ void __launch_bounds__(kThreads) row_short_kernel(const __grid_constant__ Job j) {
+__global__ void __launch_bounds__(kThreads, 3) row_short_kernel(const __grid_constant__ Job j) {
   PoolSmem& sm = *pool_smem(j.t.pool);
   load_exp_table(sm.tab);
   __syncthreads();
@@ -1354,7 +1449,9 @@ __global__ void __launch_bounds__(kThreads) row_short_kernel(const __grid_consta
   if (row0 + warp < j.t.rows) {
     unsigned long long* pool = sm.e() + warp * kShortRoom;
     double* w = reinterpret_cast<double*>(sm.e() + kWarps * kShortRoom) + warp * kShortK;
-    done = finish_short(j, row_ask(j, row0 + warp), row0 + warp, pool, w, sm.tab);
+    const int row = row0 + warp;
+    done = finish_short(j, row_ask(j, row), RowView<T>(j.t.logits, row, j.t.stride, j.t.V), row,
+                        pool, w, sm.tab);
   }
 #pragma unroll 1
   for (int q = 0; q < kWarps; ++q)
@@ -2044,15 +2141,19 @@ __device__ void deep_row(const SampleJob& j, int row, const RowLeft& left, int c
 template <typename T, int kBlock>
 __device__ void deep_row(const TopJob& j, int row, const RowLeft& left, int ctas, DeepSmem& sm) {
   const float m = left.m;
-  Deep<T, kBlock> d(sm, RowView<T>(j.t.logits, row, j.t.stride, j.t.V), m, 1.0, ctas);
+  const double iT = 1.0 / double(j.temp);
+  Deep<T, kBlock> d(sm, RowView<T>(j.t.logits, row, j.t.stride, j.t.V), m, iT, ctas);
   d.cut_top_k(uint32_t(j.k));
   if (threadIdx.x == 0) sm.n = 0u;
   d.sync();
   DeepSmem& f = d.first();
+  double S = 0.0, none = 0.0;
   d.each([&](float x, uint32_t key, int id) {
+    if (j.lse) S += d.w(x);
     if (d.in(key, id)) f.push(f32_key(x), id);
   });
-  d.sync();
+  d.sum2(S, none);  // (with a barrier of the blocks that share the row)
+  if (j.lse && d.rank == 0 && threadIdx.x == 0) write_lse(j, row, m, iT, S);
   if (d.rank == 0) {
     const int n = min(int(sm.n), kDeepCap), N = pow2_at_least(n);
     for (int q = n + int(threadIdx.x); q < N; q += kBlock) sm.e[q] = 0ull;

@@ -315,7 +315,9 @@ spec_status spec_sample(const void* logits, spec_dtype dtype, int rows, int V, i
  * is kept as for distillation.
  *   ids [rows][k] int32 out, values [rows][k] float out: the logits as they are. Entries of
  *     -inf are left out: a row with fewer than k others ends in id -1, value -inf.
- *   lse [rows] float out or NULL: log sum_v exp(l_v / temp) over the whole row.
+ *   lse [rows] float out or NULL: log sum_v exp(l_v / temp) over the whole row, within 2^-24 |lse|
+ *     and 4e-6; where the k entries hold all of the row's mass but 9e-7 of it, within 2^-24 |lse| and
+ *     2^-24, so that a list that holds it all leaves no rho below.
  * A row that holds NaN or +inf or is entirely -inf gets ids -1, values NaN and lse NaN.
  * 1 <= k <= V, k <= SPEC_MAX_TOP_LOGITS; temp finite and > 0. */
 #define SPEC_MAX_TOP_LOGITS 256

@@ -84,3 +84,78 @@ def test_a_log_sum_exp_that_is_not_the_list_s_own(V, dtype, T, off, rows):
     for got in (grad, both_grad):
         lim = step * rg.abs() + (1 + step) * 1e-5 * scale + 2e-38
         assert ((got.double().cpu() - rg).abs() <= lim).all()
+
+
+# ------------------------------------------------------------------------- the log-sum-exp of top logits
+def few_allowed(rows, V, dtype, keep, kind, seed=0):
+    """Rows of which `keep` tokens are allowed: anywhere, or side by side; the others -inf, the type's
+    lowest value, or far down."""
+    g = torch.Generator().manual_seed(seed * 7 + V)
+    x = torch.randn((rows, V), generator=g) * 2.0
+    if kind.startswith("beside"):
+        first = torch.randint(0, V - keep + 1, (rows, 1), generator=g)
+        col = torch.arange(V)[None]
+        on = (col >= first) & (col < first + keep)
+    else:
+        on = torch.zeros((rows, V), dtype=torch.bool)
+        for r in range(rows):
+            on[r, torch.randperm(V, generator=g)[:keep]] = True
+    if kind.endswith("far"):
+        return torch.where(on, x, x - 70.0).to(dtype).cuda(), on.cuda()
+    out = -math.inf if kind.endswith("masked") else torch.finfo(dtype).min
+    x = torch.where(on, x, out)
+    if kind.startswith("log"):
+        x = torch.where(on, torch.log_softmax(torch.where(on, x, -math.inf), 1), out)
+    return x.to(dtype).cuda(), on.cuda()
+
+
+@pytest.mark.parametrize("rows", [3, 60, 470])
+@pytest.mark.parametrize("V,dtype,k,keep,kind,T", [
+    (300, F32, 64, 64, "log masked", 1.0), (300, F32, 256, 200, "log lowest", 1.0),
+    (33000, BF16, 64, 40, "masked", 0.7), (33000, BF16, 64, 64, "lowest", 1.0),
+    (20000, F32, 256, 256, "log masked", 1.0), (70000, BF16, 256, 200, "beside masked", 1.0),
+    (40000, F32, 256, 250, "beside far", 1.0), (70000, BF16, 256, 250, "beside far", 1.3),
+    (200, F32, 200, 200, "log masked", 1.0), (40000, BF16, 50, 400, "far", 1.0)])
+def test_top_logits_log_sum_exp_is_exact_where_the_list_holds_the_mass(rows, V, dtype, k, keep, kind, T):
+    """Off by its rounding to float32 (half a step, 2^-24 of itself) and by its sum's float32 weights:
+    9e-7 and 8.3e-8 log2 V of the sum (2.6e-6), of which at most 1/128 counts (2.1e-8) where the list
+    leaves less than 9e-7 of the mass."""
+    x, _ = few_allowed(rows, V, dtype, keep, kind)
+    ids, val, lse = sv.spec_top_logits(x, k, T)
+    T = float(np.float32(T))
+    want = torch.logsumexp(x.double() / T, 1)
+    outside = 1.0 - (val.double() / T - want[:, None]).exp().sum(1)
+    lim = 2.0 ** -24 * want.abs() + torch.where(outside < 9e-7, 2.1e-8, 2.6e-6)
+    assert ((lse.double() - want).abs() <= lim).all(), ((lse.double() - want).abs() / lim).max()
+    top = torch.sort(x.float(), dim=1, descending=True, stable=True)
+    torch.testing.assert_close(val, top.values[:, :k], rtol=0, atol=0)
+    real = top.values[:, :k] > -math.inf
+    assert torch.equal(ids, torch.where(real, top.indices[:, :k], -1).to(torch.int32))
+
+
+@pytest.mark.parametrize("rows,V,keep,k,kind", [(4000, 300, 40, 64, "log masked"), (3000, 200, 200, 200, "log masked"),
+                                                (12, 30000, 100, 128, "log masked")])
+def test_top_logits_that_hold_all_the_mass_leave_no_rest(rows, V, keep, k, kind):
+    """A teacher and a student that allow the same tokens, all of them listed: the student has no
+    mass outside the list, and with the list's own log-sum-exp the teacher has none there either."""
+    t, on = few_allowed(rows, V, F32, keep, kind)
+    ids, val, lse = sv.spec_top_logits(t, k, 1.0)
+    g = torch.Generator().manual_seed(1)
+    x = torch.where(on, torch.randn((rows, V), generator=g).cuda(), -math.inf)
+    loss, stats = sv.spec_distill_loss(x, ids, val, lse, 1.0)
+    grad = sv.spec_distill_grad(x, ids, val, lse, 1.0, stats)
+    both_loss, both_grad = sv.spec_distill_loss_grad(x, ids, val, lse, 1.0)
+    for got in (loss, both_loss, grad, both_grad):
+        assert torch.isfinite(got).all()
+    check(x[:200], ids[:200], val[:200], lse[:200])
+
+
+@pytest.mark.parametrize("rows", [4, 470])
+def test_top_logits_are_deterministic(rows):
+    """Bit for bit, whatever order the lists were filled in."""
+    x = make(rows, 40000, BF16, "zipf")
+    first = None
+    for _ in range(6):
+        got = sv.spec_top_logits(x, 64, 1.0)
+        first = first or got
+        assert all(torch.equal(a, b) for a, b in zip(got, first))
