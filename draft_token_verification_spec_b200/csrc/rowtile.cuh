@@ -230,20 +230,21 @@ __device__ __forceinline__ float warp_sum_f32(float x) {
 struct Log2Scale {
   float hi, lo;
 };
+// The largest scale that a float holds (a temperature below 2^-127 counts as about that).
+constexpr double kMostScale = 3e38;
 // On the host, for a call's one temperature.
 inline Log2Scale log2_scale(double T) {
-  const double c = fmin(1.4426950408889634074 / T, 1e30);  // beyond, every weight but the
-                                                           // largest entry's is 0 either way
+  const double c = fmin(1.4426950408889634074 / T, kMostScale);
   float hi = float(c);
   if (double(hi) >= c) hi = nextafterf(hi, 0.0f);
   return Log2Scale{hi, fmaxf(float(c - double(hi)), 1.4e-45f)};
 }
-// For a row's own temperature, in float32: hi is the rounded quotient less a step of 2^-22 of it,
+// For a row's own temperature, in float32: hi is the rounded quotient less 2^-21 of it,
 // lo the remainder, off by 2^-24 of itself (2^-46 of c).
 __device__ __forceinline__ Log2Scale log2_scale_row(float T) {
   constexpr float L = 1.44269502f, Lr = 1.92596303e-8f;  // log2(e) = L + Lr
   if (!(T > 1.5e-30f && T < 1e30f)) {
-    const double c = fmin(1.4426950408889634074 / double(T), 1e30);
+    const double c = fmin(1.4426950408889634074 / double(T), kMostScale);
     const float h = __double2float_rd(c * (1.0 - 1e-7));
     return Log2Scale{h, fmaxf(float(c - double(h)), 1.4e-45f)};
   }
@@ -290,11 +291,11 @@ __device__ __forceinline__ float vec_exp_sum(const uint4& w, float m, const Log2
 // place.
 struct DoubleWeight {
   double md, c64;
-  float m, cf;
+  float m, least;     // x - m > least: weights above 2^-1000 (-inf where no float lies below that)
   const double* tab;  // 2^(j/64), 64 entries in shared memory
   __device__ __forceinline__ DoubleWeight(float m_, double iT, const double* tab_)
       : md(double(m_)), c64(iT * 92.33248261689366), m(m_),
-        cf(float(fmin(iT * 1.4426950408889634, 1e30))), tab(tab_) {}
+        least(float(-1000.0 * 0.6931471805599453 / iT)), tab(tab_) {}
   __device__ __forceinline__ double operator()(float x) const {
     constexpr double kMagic = 6755399441055744.0;  // 1.5 2^52
     constexpr double L = 0.010830424696249145;     // ln2 / 64
@@ -308,7 +309,7 @@ struct DoubleWeight {
     p = fma(p, r, L);
     double t = tab[n & 63];
     t = fma(t, p * r, t);
-    const bool on = (x - m) * cf > -1000.0f;
+    const bool on = x - m > least;
     return __hiloint2double(on ? __double2hiint(t) + ((n >> 6) << 20) : 0,
                             on ? __double2loint(t) : 0);
   }

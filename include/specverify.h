@@ -288,7 +288,9 @@ spec_status spec_verify_chain_noalloc(const void* target_logits, const void* dra
  * (in entries, row_stride >= V; e.g. the first V entries of a padded vocabulary). Rows may
  * start at any multiple of the element size; what lies between them is neither read nor
  * written. A workspace belongs to one call at a time: calls that may overlap (other streams,
- * graphs replayed at once) each need their own. */
+ * graphs replayed at once) each need their own.
+ * At the ends of float's range: an entry whose difference from the row's largest overflows it weighs
+ * 0 at any temperature, and a temperature below 2^-127 may count as 2^-127. */
 
 /* Draws one token per row: temperature -> top-k -> softmax -> top-p -> min-p -> renormalise,
  * then the inverse-CDF draw of spec_verify_chain.

@@ -159,3 +159,26 @@ def test_top_logits_are_deterministic(rows):
         got = sv.spec_top_logits(x, 64, 1.0)
         first = first or got
         assert all(torch.equal(a, b) for a, b in zip(got, first))
+
+
+# ------------------------------------------------------------------------- temperatures near nothing
+@pytest.mark.parametrize("T", [1e-37, 3e-35, 1e-33, 1e-31])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_logits_and_temperatures_near_the_smallest_number(T, dtype):
+    """Weights depend on the logits' differences over the temperature alone, however small both are.
+    Tolerances as in the calls' own tests. (The logits of the smallest are normal numbers but for
+    those within 0.1 of nothing, held to 1e-7 of T.)"""
+    x = make(5, 900, F32).mul(T).to(dtype)
+    u = uniforms(5)
+    for st in (dict(), dict(k=30), dict(p=0.9), dict(q=0.1), dict(k=200, p=0.8, q=0.001)):
+        check_sample(x, u, T, **st)
+    row_T = torch.full((5,), T, device="cuda")
+    check_sample(x, u, row_T, 0, 0.9)
+    check_top(x, 20, T)
+    ids, val, lse = teacher(x, 20, T=T, spread=2.0 * T)
+    check(x, ids, val, lse, T, torch.full((5,), T, device="cuda"))     # (gradients of (s - t) T / T)
+    check(x, ids, val, None, T, torch.full((5,), T, device="cuda"))
+    y = make(5, 40000, F32).mul(T).to(dtype)       # rows of several tiles, nuclei longer than a pool
+    check_sample(y, u, T, 0, 0.99)
+    check_sample(y, u, T)
+    check_top(y, 100, T)
