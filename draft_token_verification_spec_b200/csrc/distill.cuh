@@ -256,8 +256,9 @@ __device__ __forceinline__ ListSide weigh_list(int k, double iT, const int32_t* 
     scale = 1.0 / ta;
     l.mass = 1.0;
   }
-  // sum t (a / T - x / T) - log_t sum t
-  l.cross = any ? ex * scale - l.log_t * l.mass : 0.0;
+  // sum t (a / T - x / T) - log_t sum t (scale 0: all masses are below a double's smallest, and a
+  // masked x asks for nothing)
+  l.cross = any && scale > 0.0 ? ex * scale - l.log_t * l.mass : 0.0;
   l.flags |= bad ? 1 : 0;
   return l;
 }

@@ -182,3 +182,19 @@ def test_logits_and_temperatures_near_the_smallest_number(T, dtype):
     check_sample(y, u, T, 0, 0.99)
     check_sample(y, u, T)
     check_top(y, 100, T)
+
+
+@pytest.mark.parametrize("rows,V,dtype", [(3, 5000, F32), (200, 5000, BF16), (60, 40000, BF16), (2, 150000, F32)])
+def test_teacher_masses_of_nothing_ask_for_nothing(rows, V, dtype):
+    """A log-sum-exp so far above the list that its masses are 0 in double: all mass lies outside, and
+    a listed token that the student cannot give costs nothing. The loss is -log sigma, within the 1e-5
+    of test_gpu_distill.py."""
+    x = make(rows, V, dtype)
+    ids, val, lse = teacher(x, 8, short=False)
+    x[0, ids[0].long()] = -math.inf
+    lse = torch.where(torch.arange(rows, device="cuda") % 3 == 2, lse, 2000.0)
+    loss, _, _ = check(x, ids, val, lse)
+    off = x.double().scatter(1, ids.long(), -math.inf)
+    want = torch.logsumexp(x.double(), 1) - torch.logsumexp(off, 1)
+    far = lse == 2000.0
+    assert ((loss.double() - want)[far].abs() < 1e-5).all()
