@@ -594,7 +594,8 @@ __global__ void __launch_bounds__(kThreads, 6) distill_row_kernel(
   tile_arrived();
   const DistillPart mine = weigh_unlisted<T>(sm.marks, w, j.c, bad);
   if (lane < to) cl.map_shared_rank(&sm, unsigned(lane))->part[tile * kWarps + warp] = mine;
-  const float gT = kGrad ? (j.grad_loss ? j.grad_loss[row] : 1.0f) * float(j.iT) : 0.0f;
+  const float g = kGrad && j.grad_loss ? j.grad_loss[row] : 1.0f;
+  const float gT = g * float(j.iT);  // (g 0: not looked at, 1 / T may be infinite here)
   if (!kList) asm volatile("griddepcontrol.wait;" ::: "memory");
   const ListSide* l = kList ? &sm.list : j.lists + row;
   ListSide ls;
@@ -630,9 +631,9 @@ __global__ void __launch_bounds__(kThreads, 6) distill_row_kernel(
     if (inv) iZ = NAN;
     if (none) mr = 0.0f;
     T* out = static_cast<T*>(j.grad) + (long long)row * j.grad_stride;
-    store_unlisted(rv, out, tile, n, w, mr, j.c, f, gT == 0.0f);
+    store_unlisted(rv, out, tile, n, w, mr, j.c, f, g == 0.0f);
     __syncthreads();
-    if (here && gT != 0.0f) {
+    if (here && g != 0.0f) {
       // (the exponent in double: a_j / T and log_t may be large and near each other)
       const float t = ex2(float((double(a) * j.iT - ls.log_t) * 1.4426950408889634));
       const float s = (x > -INFINITY ? weight_f(x, m, j.c) : 0.0f) * iZ;  // NaN: in error

@@ -198,3 +198,19 @@ def test_teacher_masses_of_nothing_ask_for_nothing(rows, V, dtype):
     want = torch.logsumexp(x.double(), 1) - torch.logsumexp(off, 1)
     far = lse == 2000.0
     assert ((loss.double() - want)[far].abs() < 1e-5).all()
+
+
+@pytest.mark.parametrize("rows,V,dtype", [(5, 3000, F32), (200, 3000, BF16), (60, 40000, BF16), (2, 150000, F32)])
+@pytest.mark.parametrize("T", [1e-39, 1.0, 3e38])
+def test_no_gradient_is_asked_of_some_rows(rows, V, dtype, T):
+    """grad_loss 0 gives gradient 0 at every temperature, whatever the row holds."""
+    x = make(rows, V, dtype)
+    ids, val, lse = teacher(x, 8)
+    g = (torch.arange(rows, device="cuda") % 2).float()
+    x[0, 3] = math.nan
+    x[2 % rows, 4] = math.inf
+    _, stats = sv.spec_distill_loss(x, ids, val, lse, T)
+    grads = [sv.spec_distill_grad(x, ids, val, lse, T, stats, g),
+             sv.spec_distill_loss_grad(x, ids, val, lse, T, g)[1]]
+    for grad in grads:
+        assert (grad[::2] == 0.0).all()
