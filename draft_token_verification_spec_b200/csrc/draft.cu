@@ -101,11 +101,13 @@ cudaError_t launch(K kernel, const Job& j, unsigned clusters, int ctas, int thre
 }
 
 // More than the default 48 KB of shared memory for a kernel, its own included, asked for on every
-// launch: the attribute belongs to the current device.
+// launch: the attribute belongs to the current device. Always for `most`, the most that any launch of
+// the kernel takes: another thread's call with a smaller pool must not lower it between this and a
+// launch, nor below what a captured one takes.
 template <typename K>
-cudaError_t allow_smem(K kernel, size_t bytes) {
+cudaError_t allow_smem(K kernel, size_t bytes, size_t most) {
   if (bytes <= 40 * 1024) return cudaSuccess;
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(most));
 }
 
 // Entries that top-k keeps of every row, where that is known here (V: all, or not known).
@@ -120,14 +122,14 @@ int kept_by_all(const sv::SampleJob& j) {
 template <typename T, typename Job, typename Deep>
 cudaError_t launch_rows(Job j, Deep deep, cudaStream_t s) {
   static_assert(sizeof(sv::DeepSmem) <= sizeof(sv::PoolSmem) + 2 * 1024 * 8, "one memory for both");
-  const size_t pool = sv::pool_bytes(j.t.pool);
+  const size_t pool = sv::pool_bytes(j.t.pool), most_pool = sv::pool_bytes(sv::kPoolCap);
   // a few rows get eight blocks each whatever their tiles: a row that its pool does not settle is
   // gone over by all of them (48,288 entries: 110 -> 84 us, against 2 to 4 blocks)
   if (j.t.rows <= 148 / 8) j.t.blocks = 8;
   if ((long long)j.t.rows * j.t.blocks <= 148LL * 2) {
     auto kernel = sv::row_kernel<T, Job>;
     const size_t smem = std::max(pool, sizeof(sv::TileSmem));
-    const cudaError_t e = allow_smem(kernel, smem);
+    const cudaError_t e = allow_smem(kernel, smem, std::max(most_pool, sizeof(sv::TileSmem)));
     if (e != cudaSuccess) return e;
     return launch(kernel, j, unsigned(j.t.rows), j.t.blocks, kThreads, smem, false, s);
   }
@@ -138,7 +140,7 @@ cudaError_t launch_rows(Job j, Deep deep, cudaStream_t s) {
   auto finish = brief ? sv::row_short_kernel<T, Job> : sv::row_finish_kernel<T, Job>;
   const size_t smem = brief ? sv::short_bytes(j.t.pool) : pool;
   const int blocks = brief ? (j.t.rows + sv::kWarps - 1) / sv::kWarps : j.t.rows;
-  e = allow_smem(finish, smem);
+  e = allow_smem(finish, smem, brief ? sv::short_bytes(sv::kPoolCap) : most_pool);
   if (e != cudaSuccess) return e;
   // (let in early, a few blocks would share the SMs that are free first, and each takes longer: 64
   // rows of 128,256 57 us instead of 51; many gain, 2,048 rows 152 instead of 158)

@@ -3,7 +3,9 @@ log-sum-exps that do not belong to their list, temperatures near the smallest nu
 threads, outputs left out. Tolerances stand beside each test."""
 from __future__ import annotations
 
+import ctypes
 import math
+import threading
 
 import numpy as np
 import pytest
@@ -214,3 +216,53 @@ def test_no_gradient_is_asked_of_some_rows(rows, V, dtype, T):
              sv.spec_distill_loss_grad(x, ids, val, lse, T, g)[1]]
     for grad in grads:
         assert (grad[::2] == 0.0).all()
+
+
+# ------------------------------------------------------------------------- several host threads
+def hammer(calls, times):
+    """Each call (a function of the C ABI and its arguments; the interpreter's lock is released inside)
+    over and over on a thread and a stream of its own. Returns the statuses that were not 0."""
+    bad = []
+
+    def run(fn, make_args):
+        stream = torch.cuda.Stream()
+        args = make_args() + [ctypes.c_void_p(stream.cuda_stream)]
+        torch.cuda.synchronize()
+        for i in range(times):
+            st = fn(*args)
+            if st:
+                bad.append(st)
+            if i % 200 == 199:
+                stream.synchronize()
+
+    threads = [threading.Thread(target=run, args=c) for c in calls]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    return bad
+
+
+def test_calls_of_different_pools_from_several_threads():
+    """Calls whose finishing takes different amounts of shared memory, at once: what one asks for must
+    not be taken away by another before it launches."""
+    R, V = 1, 500000
+    x, u = make(R, V, BF16), uniforms(R)
+    lib, p = sv.lib(), lambda t: ctypes.c_void_p(t.data_ptr())  # noqa: E731
+    kept = []
+
+    def sample(k, top_p):
+        def args():
+            n = sv.spec_sample_workspace_size(R, V)
+            ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+            tok = torch.empty(R, dtype=torch.int32, device="cuda")
+            kept.append((k, top_p, tok, ws))
+            return [p(x), 1, R, V, V, p(u), 1.0, k, top_p, 0.0, None, None, None, None, p(tok), None,
+                    p(ws), n]
+        return args
+
+    calls = [(lib.spec_sample, sample(*kw)) for kw in ((256, 1.0), (0, 0.9), (256, 0.8), (0, 0.7))]
+    assert hammer(calls, 20000) == []
+    for k, top_p, tok, _ in kept:
+        assert tok.tolist() == ref.sample_rows(x, u, 1.0, k, top_p, 0.0)[0].tolist()
