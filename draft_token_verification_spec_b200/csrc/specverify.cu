@@ -401,8 +401,10 @@ spec_status verify_tree(const void* target_logits, spec_dtype dtype, int B, int 
 template <int R>
 cudaError_t launch_commit(const sv::LsCommitJob& j, cudaStream_t s) {
   const size_t dyn = sv::lstate_commit_smem(j.S, 16 * R);
+  // (the most any call takes: another thread's smaller call must not lower it before this launch)
   cudaError_t e = cudaFuncSetAttribute(sv::lstate_commit_kernel<R>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, int(dyn));
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       int(sv::lstate_commit_smem(sv::kLsMaxSteps, 16 * R)));
   if (e != cudaSuccess) return e;
   const long long blocks = (long long)j.B * j.H * j.tiles;
   sv::lstate_commit_kernel<R><<<unsigned(blocks), kThreads, dyn, s>>>(j);
@@ -610,14 +612,17 @@ spec_status spec_verify_tree_sampling(const void* target_logits, const void* dra
   tj.accepted_len = accepted_len;
   tj.next_token = next_token;
   const size_t dyn = size_t(N) * 20 + 16;  // normalisers (double), child lists, path
+  // allowed for the most any call takes: another thread's smaller call must not lower it before this
+  // launch
+  const size_t most = size_t(SPEC_MAX_TREE_NODES) * 20 + 16;
   cudaError_t e;
   if (dtype == SPEC_BF16) {
     e = cudaFuncSetAttribute(sv::tree_sample_kernel<__nv_bfloat16>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, int(dyn));
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, int(most));
     if (e == cudaSuccess) sv::tree_sample_kernel<__nv_bfloat16><<<B, kThreads, dyn, s>>>(tj);
   } else {
     e = cudaFuncSetAttribute(sv::tree_sample_kernel<float>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, int(dyn));
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, int(most));
     if (e == cudaSuccess) sv::tree_sample_kernel<float><<<B, kThreads, dyn, s>>>(tj);
   }
   if (e != cudaSuccess) return SPEC_ERR_CUDA;
@@ -728,8 +733,10 @@ spec_status spec_linear_state_factors(const float* alpha, const float* beta, con
     return SPEC_ERR_UNSUPPORTED;
   sv::LsFactorJob j = {alpha, beta, keys, values, B, H, S, dk, dv, w, u, gamma};
   const size_t dyn = sv::lstate_factors_smem(S, dk);
+  // (the most any call takes, as in launch_commit)
   if (cudaFuncSetAttribute(sv::lstate_factors_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           int(dyn)) != cudaSuccess)
+                           int(sv::lstate_factors_smem(sv::kLsMaxSteps, sv::kLsMaxDk))) !=
+      cudaSuccess)
     return SPEC_ERR_CUDA;
   sv::lstate_factors_kernel<<<unsigned(B * H), kThreads, dyn,
                               static_cast<cudaStream_t>(stream)>>>(j);

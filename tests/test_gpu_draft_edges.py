@@ -266,3 +266,27 @@ def test_calls_of_different_pools_from_several_threads():
     assert hammer(calls, 20000) == []
     for k, top_p, tok, _ in kept:
         assert tok.tolist() == ref.sample_rows(x, u, 1.0, k, top_p, 0.0)[0].tolist()
+
+
+def test_linear_state_factors_of_different_lengths_from_several_threads():
+    """The same of the state's factors: rounds of 1 and of 32 steps at once."""
+    B, H, dk, dv = 1, 1, 256, 8
+    lib, p = sv.lib(), lambda t: ctypes.c_void_p(t.data_ptr())  # noqa: E731
+    g = torch.Generator().manual_seed(2)
+    kept = []
+
+    def factors(S):
+        def args():
+            alpha, beta = (torch.rand((B, H, S), generator=g).cuda() * 0.1 + 0.9 for _ in range(2))
+            keys = torch.nn.functional.normalize(torch.randn((B, H, S, dk), generator=g), dim=3).cuda()
+            values = torch.randn((B, H, S, dv), generator=g).cuda()
+            out = [torch.empty_like(keys), torch.empty_like(values), torch.empty_like(alpha)]
+            kept.append((alpha, beta, keys, values, out))
+            return [p(alpha), p(beta), p(keys), p(values), B, H, S, dk, dv] + [p(o) for o in out]
+        return args
+
+    fn = lib.spec_linear_state_factors
+    assert hammer([(fn, factors(S)) for S in (32, 1, 32, 17)], 20000) == []
+    for *inputs, out in kept:
+        for a, b in zip(out, sv.spec_linear_state_factors(*inputs)):
+            assert torch.equal(a, b)
