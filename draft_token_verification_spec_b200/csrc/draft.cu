@@ -58,8 +58,9 @@ int blocks_of(int n) {
   return (n + each - 1) / each;
 }
 
-int sample_cap(int n) { return sv::list_cap(sv::kMaxJ, n); }
-int top_cap(int k, int n) { return sv::list_cap(sv::list_aim(k, n), n); }
+// (a list never holds more than the row)
+int sample_cap(int V, int n) { return std::min(V, sv::list_cap(sv::kMaxJ, n)); }
+int top_cap(int k, int V, int n) { return std::min(V, sv::list_cap(sv::list_aim(k, n), n)); }
 
 sv::TileJob tile_job(const void* logits, long long stride, int rows, int V, int n, int cap,
                      int pool, void* workspace) {
@@ -251,8 +252,8 @@ extern "C" {
 size_t spec_sample_workspace_size(int rows, int V) {
   if (rows <= 0 || V <= 0 || V > SPEC_MAX_VOCAB) return 0;
   const int n2 = tiles_of(V, 2), n4 = tiles_of(V, 4);
-  const size_t a = tile_layout(rows, n2, sample_cap(n2)).total;
-  const size_t b = tile_layout(rows, n4, sample_cap(n4)).total;
+  const size_t a = tile_layout(rows, n2, sample_cap(V, n2)).total;
+  const size_t b = tile_layout(rows, n4, sample_cap(V, n4)).total;
   return a > b ? a : b;
 }
 
@@ -273,7 +274,7 @@ spec_status spec_sample(const void* logits, spec_dtype dtype, int rows, int V, i
   const int n = tiles_of(V, elem_bytes(dtype));
   // a top_k that holds for every row tells the pool's size
   const int want = !row_top_k && top_k >= 1 && top_k < V ? top_k : -1;
-  sv::SampleJob j = {tile_job(logits, row_stride, rows, V, n, sample_cap(n),
+  sv::SampleJob j = {tile_job(logits, row_stride, rows, V, n, sample_cap(V, n),
                               sv::pool_cap(want, n), workspace),
                      uniforms, temp, top_p, min_p, top_k,
                      row_temp, row_top_k, row_top_p, row_min_p, tokens, probs};
@@ -286,8 +287,8 @@ size_t spec_top_logits_workspace_size(int rows, int V, int k) {
   if (rows <= 0 || V <= 0 || V > SPEC_MAX_VOCAB || k <= 0 || k > V || k > SPEC_MAX_TOP_LOGITS)
     return 0;
   const int n2 = tiles_of(V, 2), n4 = tiles_of(V, 4);
-  const size_t a = tile_layout(rows, n2, top_cap(k, n2)).total;
-  const size_t b = tile_layout(rows, n4, top_cap(k, n4)).total;
+  const size_t a = tile_layout(rows, n2, top_cap(k, V, n2)).total;
+  const size_t b = tile_layout(rows, n4, top_cap(k, V, n4)).total;
   return a > b ? a : b;
 }
 
@@ -303,7 +304,7 @@ spec_status spec_top_logits(const void* logits, spec_dtype dtype, int rows, int 
       workspace_bytes < spec_top_logits_workspace_size(rows, V, k))
     return SPEC_ERR_WORKSPACE;
   const int n = tiles_of(V, elem_bytes(dtype));
-  sv::TopJob j = {tile_job(logits, row_stride, rows, V, n, top_cap(k, n), sv::pool_cap(k, n),
+  sv::TopJob j = {tile_job(logits, row_stride, rows, V, n, top_cap(k, V, n), sv::pool_cap(k, n),
                            workspace),
                   k, temp, sv::log2_scale(double(temp)), ids, values, lse};
   cudaStream_t s = static_cast<cudaStream_t>(stream);

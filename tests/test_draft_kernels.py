@@ -4,6 +4,7 @@ import re
 
 import pytest
 
+import draft_token_verification_spec_b200 as sv
 from draft_token_verification_spec_b200 import _build
 
 
@@ -40,3 +41,14 @@ def test_remote_shared_memory_is_touched_only_once_its_block_runs(file, name, bo
 
 def test_the_fused_row_kernel_is_among_them():
     assert "distill_row_kernel" in [r[1] for r in REMOTE]
+
+
+@pytest.mark.parametrize("rows,V", [(65536, 1), (65536, 64), (65536, 1000), (4096, 2048)])
+def test_workspaces_of_short_rows_hold_no_more_than_the_rows(rows, V):
+    """A row of one tile: 16 bytes, eight warps' parts of 16, and a list of 8 bytes an entry, each of
+    the three rounded up to 256 bytes for the call."""
+    _build.build()
+    most = rows * (16 + 8 * 16 + 8 * V) + 3 * 256
+    assert 0 < sv.spec_sample_workspace_size(rows, V) <= most
+    for k in {1, min(V, 50), min(V, 256)}:
+        assert 0 < sv.spec_top_logits_workspace_size(rows, V, k) <= most
