@@ -487,6 +487,11 @@ def _knob(v, name, dtype, rows, device):
     return v, None
 
 
+def _int32(v) -> int:
+    """A count as the C ABI's int: one past its range stands for its end, not for its low bits."""
+    return max(-1, min(int(v), 2**31 - 1))
+
+
 def spec_sample_workspace_size(rows: int, V: int) -> int:
     return int(lib().spec_sample_workspace_size(int(rows), int(V)))
 
@@ -518,7 +523,7 @@ def spec_sample(logits, uniforms, temp=1.0, top_k=0, top_p=1.0, min_p=0.0, token
     l = lib()
     ws = _scratch(workspace, workspace is None and l.spec_sample_workspace_size(rows, V), dev)
     _check("spec_sample", l.spec_sample(
-        t.data_ptr(), code, rows, V, stride, uniforms.data_ptr(), temp, int(top_k), top_p, min_p,
+        t.data_ptr(), code, rows, V, stride, uniforms.data_ptr(), temp, _int32(top_k), top_p, min_p,
         row_temp, row_top_k, row_top_p, row_min_p, tokens.data_ptr(), probs.data_ptr(),
         ws.data_ptr(), ws.nbytes, _raw_stream(dev.index)))
     return tokens, probs
@@ -534,15 +539,16 @@ def spec_top_logits(logits, k, temp=1.0, ids=None, values=None, lse=None, worksp
     Returns (ids int32 [rows, k], values float32 [rows, k], lse float32 [rows]: the log-sum-exp
     of logits / temp over the row)."""
     t, code, rows, V, stride = _rows(logits)
-    dev, k = t.device, int(k)
+    dev, k = t.device, _int32(k)
     if not _here(stream, dev):
         return _there(spec_top_logits, stream, dev, (logits, k, temp, ids, values, lse, workspace))
+    kept = max(0, min(k, SPEC_MAX_TOP_LOGITS))   # (the call refuses any other k)
     if ids is None:
-        ids = torch.empty((rows, max(k, 0)), dtype=torch.int32, device=dev)
+        ids = torch.empty((rows, kept), dtype=torch.int32, device=dev)
     else:
         _like(ids, "ids", torch.int32, (rows, k), dev)
     if values is None:
-        values = torch.empty((rows, max(k, 0)), dtype=torch.float32, device=dev)
+        values = torch.empty((rows, kept), dtype=torch.float32, device=dev)
     else:
         _like(values, "values", torch.float32, (rows, k), dev)
     if lse is None:

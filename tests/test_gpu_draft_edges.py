@@ -290,3 +290,21 @@ def test_linear_state_factors_of_different_lengths_from_several_threads():
     for *inputs, out in kept:
         for a, b in zip(out, sv.spec_linear_state_factors(*inputs)):
             assert torch.equal(a, b)
+
+
+# ------------------------------------------------------------------------- the binding
+def test_counts_past_a_c_int():
+    """top_k past the range keeps all, as any top_k >= V; k past the limit is refused before its
+    outputs are made."""
+    x, u = make(3, 500, F32), uniforms(3)
+    want = sv.spec_sample(x, u)
+    for top_k in (2 ** 31, 2 ** 32 + 1, 2 ** 63, -2 ** 40):
+        got = sv.spec_sample(x, u, top_k=top_k)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    wide = torch.zeros((2048, 300), device="cuda")
+    before = torch.cuda.max_memory_allocated()
+    for k, status in ((257, -2), (2 ** 20, -1), (2 ** 31 - 1, -1), (2 ** 32 + 5, -1), (0, -1), (-3, -1), (-2 ** 40, -1)):
+        with pytest.raises(sv.SpecError) as e:
+            sv.spec_top_logits(wide, k)
+        assert e.value.status == status
+    assert torch.cuda.max_memory_allocated() - before < 64 << 20
