@@ -417,6 +417,9 @@ def spec_commit_linear_state(state, keys, w, u, gamma, steps, stream=None):
 
 
 # ------------------------------------------------------------------ the drafter's side
+# The calls take tensors' values and know nothing of autograd: a result has no graph, whether or not
+# the logits require a gradient. A training step hands spec_distill_grad's (or _loss_grad's) result on
+# by logits.backward(grad).
 def _rows(t, name="logits"):
     """A [rows, V] CUDA tensor of bfloat16 or float32 whose rows are V adjacent entries, any
     distance (>= V) apart. Returns (tensor, dtype code, rows, V, row stride)."""
@@ -582,6 +585,10 @@ def _grad_rows(grad, t):
     g, _, _, _, stride = _rows(grad, "grad")
     if g.dtype != t.dtype or g.shape != t.shape or g.device != t.device:
         raise ValueError("grad must match logits in type, shape and device")
+    if not g.is_inference():
+        # written behind autograd's back: a graph that kept these values (the logits', in place) is
+        # to notice
+        torch.autograd.graph.increment_version(g)
     return g, stride
 
 
@@ -594,7 +601,7 @@ def spec_distill_loss(logits, teacher_ids, teacher_logits, teacher_lse=None, tem
     """Distillation loss of each row of the student's logits [rows, V] against a teacher's top
     logits: teacher_ids int32 and teacher_logits float32 [rows, k], teacher_lse float32 [rows] or
     None (then the list is the teacher's whole distribution). Returns (loss float32 [rows], stats
-    float32 [rows, 4] for spec_distill_grad)."""
+    float32 [rows, 4] for spec_distill_grad), without a graph."""
     t, code, rows, V, stride = _rows(logits)
     dev = t.device
     if not _here(stream, dev):
@@ -621,7 +628,7 @@ def spec_distill_grad(logits, teacher_ids, teacher_logits, teacher_lse, temp, st
                       grad_loss=None, grad=None, stream=None):
     """Gradient of spec_distill_loss with respect to the logits, from the stats it returned;
     grad_loss float32 [rows] or None (1): the gradient with respect to each row's loss. grad may
-    be the logits themselves. Returns grad [rows, V] in the logits' type."""
+    be the logits themselves. Returns grad [rows, V] in the logits' type, for logits.backward(grad)."""
     t, code, rows, V, stride = _rows(logits)
     dev = t.device
     if not _here(stream, dev):
@@ -642,7 +649,8 @@ def spec_distill_grad(logits, teacher_ids, teacher_logits, teacher_lse, temp, st
 def spec_distill_loss_grad(logits, teacher_ids, teacher_logits, teacher_lse=None, temp=1.0,
                            grad_loss=None, loss=None, grad=None, workspace=None, stream=None):
     """spec_distill_loss and spec_distill_grad in one call, for a training step that knows
-    grad_loss beforehand (the row's weight in the mean). Returns (loss [rows], grad [rows, V])."""
+    grad_loss beforehand (the row's weight in the mean). grad may be the logits themselves. Returns
+    (loss [rows], grad [rows, V]), without a graph: logits.backward(grad) takes the step on."""
     t, code, rows, V, stride = _rows(logits)
     dev = t.device
     if not _here(stream, dev):

@@ -308,3 +308,40 @@ def test_counts_past_a_c_int():
             sv.spec_top_logits(wide, k)
         assert e.value.status == status
     assert torch.cuda.max_memory_allocated() - before < 64 << 20
+
+
+@pytest.mark.parametrize("call", ["grad", "loss_grad"])
+def test_logits_that_require_a_gradient(call):
+    """Results carry no graph; the gradient goes on by logits.backward(grad), the logits' own memory
+    taken for it too, and a graph that needs the logits it replaced says so."""
+    h = torch.randn((4, 32), device="cuda", requires_grad=True)
+    w = torch.randn((32, 1000), device="cuda")
+    ids, val, lse = teacher(make(4, 1000, F32), 10)
+
+    def gradient(z, out=None):
+        if call == "loss_grad":
+            loss, grad = sv.spec_distill_loss_grad(z, ids, val, lse, 1.0, grad=out)
+            assert not loss.requires_grad
+            return grad
+        loss, stats = sv.spec_distill_loss(z, ids, val, lse, 1.0)
+        assert not loss.requires_grad and not stats.requires_grad
+        return sv.spec_distill_grad(z, ids, val, lse, 1.0, stats, grad=out)
+
+    z = h @ w
+    grad = gradient(z)
+    assert not grad.requires_grad
+    z.backward(grad)
+    want = grad @ w.T
+    torch.testing.assert_close(h.grad, want)
+    h.grad = None
+    z = h @ w                      # (a product does not keep its result)
+    grad = gradient(z, z.detach())
+    z.backward(grad)
+    torch.testing.assert_close(h.grad, want)
+    y = (h @ w).exp()              # (an exponential does)
+    gradient(y.detach().log(), y.detach())
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()
+    with torch.inference_mode():
+        z = make(4, 1000, F32)
+        assert torch.isfinite(gradient(z, z)).all()
