@@ -345,3 +345,60 @@ def test_logits_that_require_a_gradient(call):
     with torch.inference_mode():
         z = make(4, 1000, F32)
         assert torch.isfinite(gradient(z, z)).all()
+
+
+# ------------------------------------------------------------------------- what the header says of outputs
+@pytest.mark.parametrize("rows,V,dtype,kind,T", [
+    (64, 128256, BF16, "flat", 1.0), (40, 32003, F32, "equal", 1.0), (600, 16384, BF16, "flat", 2.0),
+    (64, 50000, BF16, "normal", 4.0), (12, 151936, BF16, "zipf", 0.7)])
+def test_probabilities_of_untruncated_draws(rows, V, dtype, kind, T):
+    """A draw without truncation divides a double weight by the row's sum of float32 weights. Each is
+    within 2^-22 (ex2) and 2^-23 y ln 2 of itself, y its distance from the largest in bits, whose mean
+    over the mass is at most log2(V / S); a warp adds up to 2,048 of them (8 vectors of 8 for each of
+    32 lanes) in a tree of 3 + 3 + 5 levels, 2^-24 each, and what follows is in double. Rounded once."""
+    x, u = make(rows, V, dtype, kind), uniforms(rows)
+    tok, prob = sv.spec_sample(x, u, T)
+    rt, rp, _ = ref.sample_rows(x, u, T, 0, 1.0, 0.0)
+    z = ref.as_f64(x) / float(np.float32(T))
+    S = np.exp(z - z.max(1, keepdims=True)).sum(1)
+    lim = 2.0 ** -22 + 11 * 2.0 ** -24 + 2.0 ** -23 * math.log(2.0) * np.log2(V / S) + 2.0 ** -24 + 1e-8
+    np.testing.assert_array_equal(tok.cpu().numpy(), rt)
+    assert (np.abs(prob.cpu().numpy() / rp - 1.0) <= lim).all()
+
+
+@pytest.mark.parametrize("rows", [3, 60, 470])
+def test_outputs_left_out(rows):
+    """The C ABI's optional outputs as NULL: the others are what they are with them."""
+    V, k = 20000, 30
+    x, u = make(rows, V, BF16, "zipf"), uniforms(rows)
+    lib, p = sv.lib(), lambda t: ctypes.c_void_p(t.data_ptr())  # noqa: E731
+    stream = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    ws = torch.empty(sv.spec_sample_workspace_size(rows, V), dtype=torch.uint8, device="cuda")
+    for top_k, top_p in ((0, 1.0), (k, 1.0), (0, 0.9)):
+        tok = torch.empty(rows, dtype=torch.int32, device="cuda")
+        assert lib.spec_sample(p(x), 1, rows, V, V, p(u), 1.0, top_k, top_p, 0.0, None, None, None, None,
+                               p(tok), None, p(ws), ws.numel(), stream) == 0
+        assert torch.equal(tok, sv.spec_sample(x, u, 1.0, top_k, top_p)[0])
+    ids = torch.empty((rows, k), dtype=torch.int32, device="cuda")
+    val = torch.empty((rows, k), device="cuda")
+    ws = torch.empty(sv.spec_top_logits_workspace_size(rows, V, k), dtype=torch.uint8, device="cuda")
+    assert lib.spec_top_logits(p(x), 1, rows, V, V, k, 1.0, p(ids), p(val), None, p(ws), ws.numel(),
+                               stream) == 0
+    want = sv.spec_top_logits(x, k, 1.0)
+    assert torch.equal(ids, want[0]) and torch.equal(val, want[1])
+
+
+def test_many_rows_of_the_deep_kernel():
+    """Rows that their lists do not settle, by the thousands and few among thousands (each block takes
+    one by itself there, a cluster one here), on both sides of the 2,048 that are listed at a time."""
+    rows, V = 4500, 2000
+    x, u = make(rows, V, BF16, "normal"), uniforms(rows)
+    few = [5, 2047, 2048, 2050, 4097, 4499]
+    for deep in (few, list(range(2048)) + few, list(range(2100, 4500)), list(range(rows))):
+        k = torch.full((rows,), 20, dtype=torch.int32)
+        k[deep] = 1500
+        check_sample(x, u, 0.9, k.cuda(), 0.95, 0.0)
+        y = x.clone()
+        y[deep] = torch.round(y[deep] * 0.2)          # a few hundred equal entries at every threshold
+        check_top(y, 100)
+        check_sample(y, u, 1.0, 100)
