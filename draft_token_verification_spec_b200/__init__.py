@@ -504,7 +504,8 @@ def spec_sample(logits, uniforms, temp=1.0, top_k=0, top_p=1.0, min_p=0.0, token
     """Draw one token per row of logits [rows, V] (bfloat16 or float32, rows may be apart) with
     uniforms float32 [rows]. temp, top_k, top_p and min_p are numbers, or tensors [rows] on the
     logits' device (float32, top_k int32) with each row's own. Returns (tokens int32 [rows],
-    probs float32 [rows]: the drawn tokens' probabilities)."""
+    probs float32 [rows]: the drawn tokens' probabilities). The verify calls test drafts against q
+    under one temp, top_k and top_p a call and without min_p: draw what they are to test so."""
     t, code, rows, V, stride = _rows(logits)
     dev = t.device
     if not _here(stream, dev):

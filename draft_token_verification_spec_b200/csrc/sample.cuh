@@ -1486,7 +1486,8 @@ inline size_t short_bytes(int cap) {
 //   took 8 us of a search's 12.)
 //   The draw: double sums of the blocks' warps' adjacent parts, then of the threads' in the part
 //   that holds the target.
-// Shapes and orders of all sums are fixed; atomics only count and fill lists that are sorted.
+// Shapes and orders of all sums are fixed within a call (how many other rows are left decides whether
+// a row is summed by one block or by eight); atomics only count and fill lists that are sorted.
 constexpr int kDeepCtas = 8;
 constexpr int kDeepThreads = 512;
 constexpr int kDeepWarps = kDeepThreads / 32;

@@ -300,12 +300,17 @@ spec_status spec_verify_chain_noalloc(const void* target_logits, const void* dra
  *     The first three as in spec_verify_chain; min_p keeps the entries whose probability is at
  *     least min_p times the largest one's, 0 <= min_p <= 1 (0 disables it).
  *   tokens [rows] int32 out; probs [rows] float out or NULL: the drawn token's probability in
- *     the transformed distribution (the q(x) of the ratio test; 1 at temperature 0).
+ *     the transformed distribution (the q(x) of the ratio test; 1 at temperature 0), rounded from
+ *     double, or within 2.6e-6 of itself where nothing truncates the row.
  * temp == 0 gives the argmax, lowest id on ties; -inf entries are never drawn. The decisions
  * are taken in double, as in spec_verify_chain. A row that holds NaN or +inf, is entirely -inf,
  * or whose own setting is out of range (temp negative, NaN or infinite; top_p <= 0 or NaN;
  * min_p outside [0, 1]) gets token -1 and probability NaN. u[r] >= 1 or NaN draws the
- * largest kept id. */
+ * largest kept id.
+ * Drafts that a verify call is to test must be drawn as that call transforms q: it recomputes q
+ * from the draft logits, under one temp, top_k and top_p for its whole batch and without min_p, and
+ * reads no probs. Drafts drawn with min_p > 0, or rows of different settings verified in one call,
+ * would be tested against another q, and the output would not follow the target. */
 size_t spec_sample_workspace_size(int rows, int V);
 spec_status spec_sample(const void* logits, spec_dtype dtype, int rows, int V, int64_t row_stride,
                         const float* uniforms, float temp, int top_k, float top_p, float min_p,
