@@ -402,3 +402,87 @@ def test_many_rows_of_the_deep_kernel():
         y[deep] = torch.round(y[deep] * 0.2)          # a few hundred equal entries at every threshold
         check_top(y, 100)
         check_sample(y, u, 1.0, 100)
+
+
+# ------------------------------------------------------------------------- sizes
+def test_rows_further_apart_than_32_bits():
+    """Three rows whose starts lie 2.4 GB apart: the same as next to one another, gradients too."""
+    V, k, apart = 70001, 40, 1200000007
+    x = make(3, V, BF16, "zipf")
+    far = torch.empty(2 * apart + V + 5, dtype=BF16, device="cuda")[5:].as_strided((3, V), (apart, 1))
+    far.copy_(x)
+    u = uniforms(3)
+    for st in (dict(), dict(k=50), dict(p=0.9), dict(T=0.0), dict(k=9000)):
+        check_sample(far, u, **st)
+    check_top(far, k)
+    ids, val, lse = teacher(x, k)
+    loss, stats = sv.spec_distill_loss(far, ids, val, lse)
+    assert torch.equal(loss, sv.spec_distill_loss(x, ids, val, lse)[0])
+    want = sv.spec_distill_grad(x, ids, val, lse, 1.0, stats)
+    both = sv.spec_distill_loss_grad(x, ids, val, lse)[1]
+    assert torch.equal(sv.spec_distill_loss_grad(far, ids, val, lse, grad=far)[1], both)
+    far.copy_(x)
+    assert torch.equal(sv.spec_distill_grad(far, ids, val, lse, 1.0, stats, grad=far), want)
+
+
+def test_more_entries_than_32_bits_count():
+    """36,000 rows of 128,256 entries, and lists and gradients of as many: the last rows come out as
+    they do by themselves."""
+    R, V, k, few = 36000, 128256, 64, 40
+    g = torch.Generator(device="cuda").manual_seed(0)
+    x = torch.empty((R, V), dtype=BF16, device="cuda")
+    x[:-few].normal_(0.0, 3.0, generator=g)
+    x[-few:] = make(few, V, BF16, "zipf")
+    u = torch.rand(R, generator=g, device="cuda")
+    for top_k, top_p in ((50, 1.0), (0, 0.9), (0, 1.0)):
+        tok, prob = sv.spec_sample(x, u, 0.8, top_k, top_p)
+        rt, rp, _ = ref.sample_rows(x[-few:], u[-few:], 0.8, top_k, top_p, 0.0)
+        np.testing.assert_array_equal(tok[-few:].cpu().numpy(), rt)
+        np.testing.assert_allclose(prob[-few:].cpu().numpy(), rp, rtol=4e-6)
+    ids, val, lse = sv.spec_top_logits(x, k)
+    ri, rv, rl = ref.top_rows(x[-few:], k, 1.0)
+    np.testing.assert_array_equal(ids[-few:].cpu().numpy(), ri)
+    np.testing.assert_array_equal(val[-few:].cpu().numpy(), rv)
+    np.testing.assert_allclose(lse[-few:].cpu().numpy(), rl, rtol=2.0 ** -23, atol=2.6e-6)
+    i2, v2, l2 = teacher(x[-few:], k)
+    ids[-few:], val[-few:], lse[-few:] = i2, v2, l2
+    loss, stats = sv.spec_distill_loss(x, ids, val, lse)
+    grads = [sv.spec_distill_grad(x, ids, val, lse, 1.0, stats)[-few:].clone()]
+    both_loss, grad = sv.spec_distill_loss_grad(x, ids, val, lse, grad=x)
+    grads.append(grad[-few:])
+    rl, rg, scale = ref.distill_rows(make(few, V, BF16, "zipf"), i2, v2, l2, 1.0)
+    for got in (loss, both_loss):
+        np.testing.assert_allclose(got[-few:].cpu().numpy(), rl, rtol=2.0 ** -23, atol=1e-5)
+    for got in grads:
+        assert (np.abs(ref.as_f64(got) - rg) <= 2.0 ** -8 * np.abs(rg) + 1.01e-5 * scale + 2e-38).all()
+
+
+@pytest.mark.parametrize("rows", [3, 200])
+@pytest.mark.parametrize("V,dtype", [(5, F32), (100, BF16), (9003, BF16), (150001, F32)])
+def test_lists_longer_than_the_row_and_gradients_over_rows_apart(V, dtype, rows):
+    """Lists padded past the vocabulary, the entries in any places; the gradient over logits that are
+    cut out of wider rows, whose other entries stay."""
+    if V == 150001:
+        rows = 3
+    k = min(V, 30)
+    x = make(rows, V, dtype, "normal")
+    ids, val, lse = teacher(x, k, short=False)
+    wide_ids = torch.full((rows, 256), -1, dtype=torch.int32, device="cuda")
+    wide_val = torch.full((rows, 256), math.nan, device="cuda")     # (beside a negative id: not looked at)
+    at = torch.randperm(256, generator=torch.Generator().manual_seed(V))[:k].cuda()
+    wide_ids[:, at], wide_val[:, at] = ids, val
+    rl, rg, scale = ref.distill_rows(x, ids, val, lse, 1.0)
+    loss, stats = sv.spec_distill_loss(x, wide_ids, wide_val, lse)
+    step = torch.finfo(dtype).eps / 2
+    for call in ("grad", "both"):
+        full = torch.full((rows, V + 11), 7.0, dtype=dtype, device="cuda")
+        z = full[:, 3:V + 3]
+        z.copy_(x)
+        if call == "grad":
+            grad, got = sv.spec_distill_grad(z, wide_ids, wide_val, lse, 1.0, stats, grad=z), loss
+        else:
+            got, grad = sv.spec_distill_loss_grad(z, wide_ids, wide_val, lse, grad=z)
+        assert grad.data_ptr() == z.data_ptr()
+        assert (full[:, :3] == 7.0).all() and (full[:, V + 3:] == 7.0).all()
+        np.testing.assert_allclose(got.cpu().numpy(), rl, rtol=2.0 ** -23, atol=1e-5)
+        assert (np.abs(ref.as_f64(grad) - rg) <= step * np.abs(rg) + (1 + step) * 1e-5 * scale + 2e-38).all()
