@@ -465,6 +465,8 @@ def _there(call, stream, device, args):
     """call(*args) with the device current, and the stream (a Stream or a handle) current on it:
     what the call allocates then belongs to the stream it runs on, and is reused only after its
     work."""
+    if isinstance(stream, torch.cuda.Stream) and stream.device != device:
+        raise ValueError(f"stream must be one of {device}, got one of {stream.device}")
     with torch.cuda.device(device):
         if stream is None:
             return call(*args)

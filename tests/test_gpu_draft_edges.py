@@ -486,3 +486,18 @@ def test_lists_longer_than_the_row_and_gradients_over_rows_apart(V, dtype, rows)
         assert (full[:, :3] == 7.0).all() and (full[:, V + 3:] == 7.0).all()
         np.testing.assert_allclose(got.cpu().numpy(), rl, rtol=2.0 ** -23, atol=1e-5)
         assert (np.abs(ref.as_f64(grad) - rg) <= step * np.abs(rg) + (1 + step) * 1e-5 * scale + 2e-38).all()
+
+
+def test_streams():
+    """A stream as an object or by its handle, the default one's 0 too; one of another device is
+    refused, not left aside."""
+    x, u = make(5, 30000, BF16, "zipf"), uniforms(5)
+    want = sv.spec_sample(x, u, 0.8, 40)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream, 0, torch.cuda.current_stream(), torch.cuda.default_stream()):
+        got = sv.spec_sample(x, u, 0.8, 40, stream=stream)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    with pytest.raises(ValueError, match="stream must be one of"):
+        sv._there(lambda: None, side, torch.device("cuda", side.device.index + 1), ())
