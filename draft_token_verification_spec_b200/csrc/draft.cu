@@ -11,6 +11,8 @@
 namespace {
 
 using sv::kThreads;
+static_assert(SPEC_MAX_TOP_LOGITS <= kThreads, "finish_row: one of the k largest to a thread");
+static_assert(SPEC_MAX_TOP_LOGITS <= sv::kMaxTeacher, "a list's entries");
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 size_t up256(size_t b) { return (b + 255) / 256 * 256; }

@@ -1408,7 +1408,6 @@ __device__ void finish_row(const TopJob& j, const RowAsk& a, const RowView<T>& r
   }
   for (int i = tid; i < j.k; i += kThreads) write_top(j, row, i, i < c, sm.e()[i < c ? i : 0]);
   if (j.lse) {
-    static_assert(kMaxJ <= kThreads, "one of the k largest to a thread");
     const DoubleWeight f(sm.m, a.iT, sm.tab);
     double S = sm.s;
     const double own = tid < min(c, j.k) ? f(pool_value(sm.e()[tid])) : 0.0;

@@ -301,7 +301,7 @@ spec_status spec_verify_chain_noalloc(const void* target_logits, const void* dra
  *     least min_p times the largest one's, 0 <= min_p <= 1 (0 disables it).
  *   tokens [rows] int32 out; probs [rows] float out or NULL: the drawn token's probability in
  *     the transformed distribution (the q(x) of the ratio test; 1 at temperature 0), rounded from
- *     double, or within 2.6e-6 of itself where nothing truncates the row.
+ *     double, or within 2.7e-6 of itself where nothing truncates the row.
  * temp == 0 gives the argmax, lowest id on ties; -inf entries are never drawn. The decisions
  * are taken in double, as in spec_verify_chain. A row that holds NaN or +inf, is entirely -inf,
  * or whose own setting is out of range (temp negative, NaN or infinite; top_p <= 0 or NaN;
@@ -340,7 +340,8 @@ spec_status spec_top_logits(const void* logits, spec_dtype dtype, int rows, int 
  *   teacher_lse NULL:    t = softmax of the list's logits / temp, rho = 0;
  *   teacher_lse [rows]:  t_j = exp(a_j / temp - lse), the teacher's own probabilities, and
  *                        rho = 1 - sum_j t_j its mass outside the list, one more outcome
- *                        (0 where it is at most (|lse| + 1) 2^-23, the rounding of a float lse);
+ *                        (0 where it is at most (|lse| + 1) 2^-23, the rounding of a float lse:
+ *                        spec_top_logits' keeps to it; one from longer float sums leaves their error);
  *   loss = sum_j t_j (log t_j - log s_j) + rho (log rho - log sigma), sigma the student's mass
  *   outside the list (terms with t_j = 0 or rho = 0 are 0; +inf where the student has no mass);
  *   d loss / d z_v = (s_v - t_v) / temp listed, (s_v - rho s_v / sigma) / temp unlisted.
