@@ -40,7 +40,8 @@ struct WarpPart {
 static_assert(sizeof(WarpPart) == 16, "WarpPart is 16 bytes");
 
 // What finishing leaves to the deep kernel: whether the row is its, the row's maximum, and for a
-// nucleus that its pool holds but the float32 sum leaves open, the keys that the cut lies between.
+// nucleus that its pool holds but the float32 sum leaves open, the keys that the cut lies between
+// (top logits: the two halves of the row's sum).
 struct RowLeft {
   int32_t todo;
   float m;
@@ -900,8 +901,22 @@ __device__ __forceinline__ void write_top(const TopJob& j, int row, int i, bool 
 // again, part by part (a warp's 256 vectors of a tile): the parts that hold more than 1 / (128
 // parts) of it are read again, their entries among the k largest weigh in double, and only the rest
 // of them in float32. The other parts are 1/128 of the sum together: it is off by e / 128 < 2.1e-8.
-__device__ __forceinline__ bool sum_stands(int V, double S, double largest) {
-  return S - largest > 2.0 * sum_error(V, S) * S;
+// Whether the sum stands, by the calling warp alone (all its lanes get the answer, every warp the
+// same): float32 weights, off by less than 3e-6, tell most rows; e is under 2.6e-6. top: the `have`
+// largest entries.
+__device__ __forceinline__ bool sum_stands(const TopJob& j, double S, float m, double iT,
+                                           const double* tab, const unsigned long long* top,
+                                           int have) {
+  const int lane = threadIdx.x & 31;
+  float q = 0.0f;
+#pragma unroll 1
+  for (int i = lane; i < have; i += 32) q += weight_f(pool_value(top[i]), m, j.c);
+  if (S - double(warp_sum_f32(q)) > 1e-5 * S) return true;
+  const DoubleWeight f(m, iT, tab);
+  double d = 0.0;
+#pragma unroll 1
+  for (int i = lane; i < have; i += 32) d += f(pool_value(top[i]));
+  return S - warp_sum_f64(d) > 2.0 * sum_error(j.t.V, S) * S;
 }
 
 // The calling warp's share of that sum (each lane's is to be added): the parts and the k largest are
@@ -1151,11 +1166,7 @@ __device__ __forceinline__ bool finish_short(const TopJob& j, const RowAsk& a,
   if (!short_pool(j, a, row, pool, tab, &m, j.lse ? &s : nullptr)) return false;
   if (lane == 0) j.t.left[row] = RowLeft{0, 0.0f, 0u, 0u};
   if (j.lse) {
-    const DoubleWeight f(m, a.iT, tab);
-    double own = 0.0;
-#pragma unroll 1
-    for (int i = lane; i < j.k; i += 32) own += f(pool_value(pool[i]));
-    if (!sum_stands(j.t.V, s, warp_sum_f64(own)))
+    if (!sum_stands(j, s, m, a.iT, tab, pool, j.k))
       s = warp_sum_f64(exact_share(j.t, rv, row, m, a.iT, tab, j.c, pool, j.k, j.k, s, 0, 1));
     if (lane == 0) write_lse(j, row, m, a.iT, s);
   }
@@ -1368,9 +1379,18 @@ __device__ void finish_row(const TopJob& j, const RowAsk& a, const RowView<T>& r
                            PoolSmem& sm) {
   const int tid = threadIdx.x;
   merge_parts(j, a, row, sm);
-  if (tid == 0) j.t.left[row] = RowLeft{0, 0.0f, 0u, 0u};
+  const float m = sm.m;
+  const double S = sm.s;
+  if (tid == 0) {
+    j.t.left[row] = RowLeft{0, 0.0f, 0u, 0u};
+    if (j.lse) {  // (once the k largest are known, the sum may be taken again)
+      if (sm.bad)
+        j.lse[row] = NAN;
+      else
+        write_lse(j, row, m, a.iT, S);
+    }
+  }
   if (sm.bad) {
-    if (tid == 0 && j.lse) j.lse[row] = NAN;
     for (int i = tid; i < j.k; i += kThreads) {
       j.ids[size_t(row) * j.k + i] = -1;
       j.values[size_t(row) * j.k + i] = NAN;
@@ -1403,18 +1423,16 @@ __device__ void finish_row(const TopJob& j, const RowAsk& a, const RowView<T>& r
     }
   }
   if (c < 0) {
-    if (tid == 0) leave_row(j.t, row, sm.m);
+    // (the sum goes along where a nucleus would have its keys)
+    if (tid == 0)
+      leave_row(j.t, row, m, uint32_t(__double2loint(S)), uint32_t(__double2hiint(S)));
     return;
   }
   for (int i = tid; i < j.k; i += kThreads) write_top(j, row, i, i < c, sm.e()[i < c ? i : 0]);
-  if (j.lse) {
-    const DoubleWeight f(sm.m, a.iT, sm.tab);
-    double S = sm.s;
-    const double own = tid < min(c, j.k) ? f(pool_value(sm.e()[tid])) : 0.0;
-    if (!sum_stands(j.t.V, S, block_sum_f64(own, sm.scr)))
-      S = block_sum_f64(exact_share(j.t, rv, row, sm.m, a.iT, sm.tab, j.c, sm.e(), c, j.k, S,
-                                    tid >> 5, kWarps), sm.scr);
-    if (tid == 0) write_lse(j, row, sm.m, a.iT, S);
+  if (j.lse && !sum_stands(j, S, m, a.iT, sm.tab, sm.e(), min(c, j.k))) {
+    const double all = block_sum_f64(exact_share(j.t, rv, row, m, a.iT, sm.tab, j.c, sm.e(), c,
+                                                 j.k, S, tid >> 5, kWarps), sm.scr);
+    if (tid == 0) write_lse(j, row, m, a.iT, all);
   }
 }
 
@@ -2147,13 +2165,10 @@ __device__ void deep_row(const TopJob& j, int row, const RowLeft& left, int ctas
   if (threadIdx.x == 0) sm.n = 0u;
   d.sync();
   DeepSmem& f = d.first();
-  double S = 0.0, none = 0.0;
   d.each([&](float x, uint32_t key, int id) {
-    if (j.lse) S += d.w(x);
     if (d.in(key, id)) f.push(f32_key(x), id);
   });
-  d.sum2(S, none);  // (with a barrier of the blocks that share the row)
-  if (j.lse && d.rank == 0 && threadIdx.x == 0) write_lse(j, row, m, iT, S);
+  d.sync();
   if (d.rank == 0) {
     const int n = min(int(sm.n), kDeepCap), N = pow2_at_least(n);
     for (int q = n + int(threadIdx.x); q < N; q += kBlock) sm.e[q] = 0ull;
@@ -2161,6 +2176,17 @@ __device__ void deep_row(const TopJob& j, int row, const RowLeft& left, int ctas
     block_sort<true, kBlock>(sm.e, N);
     for (int q = threadIdx.x; q < j.k; q += kBlock)
       write_top(j, row, q, q < n, sm.e[q < n ? q : 0]);
+    const double S = __hiloint2double(int(left.hi), int(left.lo));
+    if (j.lse && !sum_stands(j, S, m, iT, sm.tab, sm.e, min(n, j.k))) {
+      const int warp = threadIdx.x >> 5;
+      const double own = warp_sum_f64(exact_share(j.t, d.rv, row, m, iT, sm.tab, j.c, sm.e, n, j.k,
+                                                  S, warp, kBlock / 32));
+      if ((threadIdx.x & 31) == 0) sm.scr[warp] = own;
+      __syncthreads();
+      double all = 0.0;
+      for (int q = 0; q < kBlock / 32; ++q) all += sm.scr[q];
+      if (threadIdx.x == 0) write_lse(j, row, m, iT, all);
+    }
   }
   d.sync();
 }
